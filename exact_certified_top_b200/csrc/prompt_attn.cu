@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_clean = o_full + 2;                    // [stage]: the V tile has been checked
   uint64_t* kv_full = v_clean + kStages;
   uint64_t* kv_empty = kv_full + kStages;
-  uint64_t* done_bar = kv_empty + kStages;
+  uint64_t* s_seen = kv_empty + kStages;             // [tile]: the unit's last s_full were seen
+  uint64_t* done_bar = s_seen + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done_bar + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   // per tile and last kBadUnits of its units: [kBadWords] keys with a value that is not
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&o_full[i], 1);
+      mbar_init(&s_seen[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -616,6 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(&kv_full[sk], c / kStages);
           if (n > 0) {
             if (ok) ok = wait(&q_full[i], nq);
+            // The softmax warps have seen the last unit's products end: a phase that
+            // completed before they looked would be lost to them, and a barrier's
+            // parity tells only neighbours apart.
+            if (ok) ok = wait(&s_seen[i], nq + 1);
             tc_fence_after();
             if (issuer && ok) {
 #pragma unroll
@@ -743,6 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&s_full[2 * i + (j & 1)], (ph >> (j & 1)) & 1, s_abort, p.err);
           if (!ok) break;
           ph ^= 1u << (j & 1);
+          tc_fence_before();                           // the last unit's loads of O
+          __syncwarp();
           if (lane == 0) mbar_arrive(&p_ready[2 * i + (j & 1)]);
           __syncwarp();
         }
@@ -802,6 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) ok = warp_wait(&s_full[2 * i + hf], (ph >> hf) & 1, s_abort, p.err);
           ph ^= 1u << hf;
         }
+        if (lane == 0) mbar_arrive(&s_seen[i]);        // the next unit's scores may come
+        __syncwarp();
         if (ok) ok = warp_wait(&o_full[i], nq & 1, s_abort, p.err);
       }
       if (ok) {

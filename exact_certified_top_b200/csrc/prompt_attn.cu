@@ -236,10 +236,11 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 // polynomial of least relative error (2.6e-6, fitted by Remez exchange; P itself
 // rounds to 2^-12 or 2^-9), times 2^n.  x is held at -127, whose factor is a zero
 // of the bits: masked scores (-infinity) and what is below 2^-126.5 weigh nothing,
-// however large the value.  NaN never comes alone: it has reached the row's
-// maximum, so the row's other weights are NaN.
+// however large the value.  NaN stays: a score of +infinity is one here (infinity
+// minus the maximum it has become), and a zero in its place would drop the key
+// and leave a row without weights.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
-  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
   const float2 r = add2(x, both(12582912.f));
   const float2 f = add2(x, fma2(r, both(-1.f), both(12582912.f)));
   float2 q = fma2(f, both(9.570102207362652e-3f), both(5.591785907745361e-2f));

@@ -386,7 +386,8 @@ void dosa_attn_destroy(dosa_attn_t h);
  * Hq] rows; lse (nullable) [Tq, Hq] fp32, contiguous.  Whole prompts (q_pos0 =
  * 0), chunks against a cached prefix and single rows per sequence alike: long
  * key ranges of few rows are split over the SMs and joined.  A row whose
- * scores are all -infinity gives zeros and lse = -infinity.  Weights (up to 2^8
+ * scores are all -infinity gives zeros and lse = -infinity, one that sees a score
+ * of +infinity or NaN gives NaN (lse too).  Weights (up to 2^8
  * in bf16, 2^15 in fp16, before they are divided by their sum) times values are
  * summed in fp32: bf16 values whose sum over the keys passes 2^119 may overflow.  out must not overlap the
  * inputs.  Workspace: dosa_attn_prompt_workspace_size of the same
@@ -439,7 +440,8 @@ dosa_status dosa_cache4_read(dosa_attn_t h, const dosa_cache4* cache, const int6
  * the out_idx of a Top-K call for the same batch: row t attends over the listed
  * keys (indices relative to the sequence's first key).  Entries that are
  * negative or beyond the row's position are left out; a key listed twice
- * counts twice.  A row with no key gives zeros and lse = -infinity.
+ * counts twice.  A row with no key gives zeros and lse = -infinity, one that sees
+ * a score of +infinity or NaN gives NaN.
  * add_weights: after the call weight[slot] has grown by the sum over the
  * batch's rows and heads of p (rows in order, so results do not depend on
  * timing); needs cache->weight.  A row and head whose lse is -infinity adds

@@ -15,9 +15,13 @@
 // two fp16 parts).  q is scaled by a power of two per column so that fp16
 // holds bf16's bits.  For the values the scale goes to the other operand:
 //   out(h,i) = sum_t (p(t,h) s(t,g)) c(t,i) + sum_t p(t,h) m(t,g)
-// p is rounded to fp16 and so is p s (2^-11 each, random).  p is kept 2^kLift
-// times larger and the scales by a power of two per warp, so that both and
-// their product stay in fp16's range down to weights of 2^-30.  Running maxima
+// p is rounded to fp16 for the second sum and p s, formed in fp32, for the first:
+// 2^-11 each.  p is kept 2^kLift times larger and the scales of each group by a
+// power of two per warp that brings the largest below 1, so that weights keep their
+// bits down to 2^-26 of the row's largest (thousands of such keys may carry a row
+// whose largest weight meets a small value) and groups of any size theirs; what
+// is lost below is half a step of 2^-24, at most 2^-37 of the largest weight per
+// key times |min|, and 2^-36 times 15 of the group's largest scale.  Running maxima
 // move only when a score exceeds them by 2^kSlack, so most slices need no
 // rescaling.
 //
@@ -49,8 +53,9 @@ constexpr int kOffV = kSlice * kVecCodes;         // key codes, value codes, key
 constexpr int kOffKp = 2 * kSlice * kVecCodes;
 constexpr int kOffVp = kOffKp + kSlice * kVecParams;
 constexpr float kSlack = 3.f;                     // log2 units a score may exceed the running maximum
-constexpr float kLift = 6.f;                      // weights are kept 2^kLift times larger: `top` is the
-                                                  // maximum minus kLift
+constexpr float kLift = 12.f;                     // weights are kept 2^kLift times larger, up to
+                                                  // 2^(kLift + kSlack) = 2^15: `top` is the maximum
+                                                  // minus kLift
 constexpr float kNegInf = -INFINITY;
 // Running maximum of a column that has seen nothing: finite, so that a score of
 // -infinity minus it is -infinity and not NaN.
@@ -138,6 +143,24 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 }
 __device__ __forceinline__ float half_lo(uint32_t w) {
   return __low2float(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Two fp32 products per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// 1 / x of a power of two.
+__device__ __forceinline__ float pow2_inverse(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+// The scales of two (scale, min) words.
+__device__ __forceinline__ __half2 scales(uint32_t a, uint32_t b) {
+  return as_half2(__byte_perm(a, b, 0x5410));
 }
 
 // Both halves that are not finite replaced by zero.
@@ -503,10 +526,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     top[n][0] = top[n][1] = kNone;
     sum[n][0] = sum[n][1] = 0.f;
   }
-  // Value scales enter as s fs, fs a power of two that brings the largest seen so
-  // far below 2^6; s_max is the scale where it has to move.
-  __half2 fs2 = __float2half2_rn(1.f);
-  float fs = 1.f, fs_inv = 1.f, s_max = 0.f;
+  // Value scales enter as s fs, fs a power of two per group of dimensions that
+  // brings the largest seen so far below 1; fs_lim (two groups per word) is the
+  // scale above which it has to move.
+  float fs[4] = {1.f, 1.f, 1.f, 1.f};
+  __half2 fs_lim[2] = {__float2half2_rn(0.f), __float2half2_rn(0.f)};
 
   // Two slices per step (one for 32 columns, where registers are short): their
   // loads, products and checks interleave.
@@ -530,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     float sc[kPair][NT][4];
     uint32_t seen[kPair][NT][2];      // halves of ones where a column sees token r, r + 8
     uint4 pa[kPair], pb[kPair];       // value parameters of tokens r, r + 8
-    __half2 vs2 = __float2half2_rn(0.f);
+    __half2 vs[2] = {__float2half2_rn(0.f), __float2half2_rn(0.f)};   // largest value scales
     bool grow = false;
 #pragma unroll
     for (int e = 0; e < kPair; ++e) {
@@ -572,32 +596,47 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       pb[e] = lds128(stage[e] + kOffVp + (r + 8) * 16);
       // a slice behind the last: its stage holds anything
       if (e > 0 && sl + e * kWarps >= n_slices) pa[e] = pb[e] = make_uint4(0, 0, 0, 0);
-      const uint32_t w[8] = {pa[e].x, pa[e].y, pa[e].z, pa[e].w, pb[e].x, pb[e].y, pb[e].z, pb[e].w};
-#pragma unroll
-      for (int g = 0; g < 8; ++g) vs2 = __hmax2(vs2, as_half2(w[g]));   // (scale, min): NaN is passed over
+      vs[0] = __hmax2(vs[0], __hmax2(scales(pa[e].x, pa[e].y), scales(pb[e].x, pb[e].y)));
+      vs[1] = __hmax2(vs[1], __hmax2(scales(pa[e].z, pa[e].w), scales(pb[e].z, pb[e].w)));
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           grow |= fmaxf(sc[e][n][i], sc[e][n][i + 2]) > top[n][i] + (kLift + kSlack);
     }
-    float vs = __low2float(vs2);
-    grow |= vs > s_max;
+    grow |= (__hgt2_mask(vs[0], fs_lim[0]) | __hgt2_mask(vs[1], fs_lim[1])) != 0;
     if (__any_sync(0xFFFFFFFFu, grow)) {
-      // new maxima, shared by the 8 lanes of a column; and the value scale's
+      // new maxima, shared by the 8 lanes of a column; and the value scales'
+      float adj[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
-      for (int o2 = 1; o2 < 32; o2 <<= 1) vs = fmaxf(vs, __shfl_xor_sync(0xFFFFFFFFu, vs, o2));
-      float adj = 1.f;
-      if (vs > s_max && vs < INFINITY) {
-        // vs 2^e in [2^5, 2^6); 2^e itself has to be an fp16 number
-        int e = 132 - (int)(__float_as_uint(vs) >> 23);
-        e = e > 15 ? 15 : e;
-        const float nf = __uint_as_float((uint32_t)(127 + e) << 23);
-        adj = nf * fs_inv;
-        fs = nf;
-        fs2 = __float2half2_rn(nf);
-        fs_inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        s_max = 64.f * fs_inv;
+      for (int i = 0; i < 2; ++i) {
+        // (an infinite scale must not hide the finite ones beside it)
+        __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+        for (int e = 0; e < kPair; ++e) {
+          m = __hmax2(m, as_half2(finite_only(as_word(
+                             i ? scales(pa[e].z, pa[e].w) : scales(pa[e].x, pa[e].y)))));
+          m = __hmax2(m, as_half2(finite_only(as_word(
+                             i ? scales(pb[e].z, pb[e].w) : scales(pb[e].x, pb[e].y)))));
+        }
+#pragma unroll
+        for (int o2 = 1; o2 < 32; o2 <<= 1)
+          m = __hmax2(m, as_half2(__shfl_xor_sync(0xFFFFFFFFu, as_word(m), o2)));
+        const float2 top2 = __half22float2(m), lim2 = __half22float2(fs_lim[i]);
+        float lim[2] = {lim2.x, lim2.y};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float v = h ? top2.y : top2.x;
+          if (v > lim[h]) {
+            // v fs in [1/2, 1); v is an fp16 number, so fs is 2^-16 .. 2^23
+            const uint32_t e = __float_as_uint(v) >> 23;
+            const float nf = __uint_as_float((253u - e) << 23);
+            adj[2 * i + h] = nf * pow2_inverse(fs[2 * i + h]);
+            fs[2 * i + h] = nf;
+            lim[h] = __uint_as_float((e + 1u) << 23);   // (2^16 becomes infinity)
+          }
+        }
+        fs_lim[i] = __floats2half2_rn(lim[0], lim[1]);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -619,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][i][j] *= k[j & 1] * adj;
+          for (int j = 0; j < 4; ++j) o[n][i][j] *= k[j & 1] * adj[i >> 1];
       }
     }
     // value words: tokens 2c, 2c + 1 and 2c + 8, 2c + 9, nibbles 16 r ..
@@ -636,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       uint32_t m0, m1;
       ldsm2t(stage[e] + kOffVp + (lane & 15) * 16, m0, m1);
       __half2 pr[NT][2];              // p of token r, r + 8; columns 2c, 2c + 1
+      float2 pf[NT][2];               // the same in fp32
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float p0 = ex2(sc[e][n][0] - top[n][0]), p1 = ex2(sc[e][n][1] - top[n][1]);
@@ -644,6 +684,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         sum[n][1] += p1 + p3;
         pr[n][0] = __floats2half2_rn(p0, p1);
         pr[n][1] = __floats2half2_rn(p2, p3);
+        pf[n][0] = make_float2(p0, p1);
+        pf[n][1] = make_float2(p2, p3);
       }
       const uint32_t ha[4] = {pa[e].x, pa[e].y, pa[e].z, pa[e].w};
       const uint32_t hb[4] = {pb[e].x, pb[e].y, pb[e].z, pb[e].w};
@@ -665,16 +707,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const uint32_t cb = __byte_perm(g < 2 ? v2.x : v2.y, g < 2 ? v3.x : v3.y,
                                         (g & 1) ? 0x7632 : 0x5410);
         const uint32_t ca8 = ca >> 8, cb8 = cb >> 8;
-        __half2 sa = __hmul2(__low2half2(as_half2(ha[g])), fs2);
-        __half2 sb = __hmul2(__low2half2(as_half2(hb[g])), fs2);
+        float sa = half_lo(ha[g]) * fs[g], sb = half_lo(hb[g]) * fs[g];
         if (!whole) {
-          const __half2 zero = __float2half2_rn(0.f);
-          sa = __hfma2(__high2half2(as_half2(ha[g])), zero, sa);
-          sb = __hfma2(__high2half2(as_half2(hb[g])), zero, sb);
+          sa = fmaf(__high2float(as_half2(ha[g])), 0.f, sa);
+          sb = fmaf(__high2float(as_half2(hb[g])), 0.f, sb);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          uint32_t wa = as_word(__hmul2(pr[n][0], sa)), wb = as_word(__hmul2(pr[n][1], sb));
+          const float2 fa = mul2(pf[n][0], make_float2(sa, sa));
+          const float2 fb = mul2(pf[n][1], make_float2(sb, sb));
+          uint32_t wa = pack_half(fa.x, fa.y), wb = pack_half(fb.x, fb.y);
           if (!whole) {
             wa &= seen[e][n][0];
             wb &= seen[e][n][1];
@@ -716,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       // sum p m of group g sits in row 2g + 1, i.e. in lanes 4 (2g + 1) + c
       const float a0 = __shfl_sync(0xFFFFFFFFu, om[n][0], 4 * (2 * g + 1) + c);
       const float a1 = __shfl_sync(0xFFFFFFFFu, om[n][1], 4 * (2 * g + 1) + c);
-      const float b = 16777216.f * fs_inv;
+      const float b = 16777216.f * pow2_inverse(fs[g]);
       float* d0 = jo + (warp * NC + n * 8 + 2 * c) * kHeadDim + 32 * g + 4 * r;
       float* d1 = d0 + kHeadDim;
       const float* e0 = o[n][2 * g];

@@ -93,3 +93,102 @@ def test_attend_a_score_of_plus_infinity_is_not_dropped(Hq, selected):
     sel = torch.arange(s, dtype=torch.int32, device="cuda")[None] if selected else None
     out, lse = at.attend(cache, q, so, sel_idx=sel, lse=True)
     assert torch.isnan(out).all() and not (lse == -math.inf).any()
+
+
+def _cache_of(k, v):
+    """A cache whose slots hold rows k, v [n, Hkv, D]."""
+    cache = binding.Cache4.empty(k.shape[1], k.shape[0])
+    for kind, x in (("k", k), ("v", v)):
+        codes, params = ref.quantise(x, kind)
+        getattr(cache, kind + "_codes").copy_(codes)
+        getattr(cache, kind + "_params").copy_(params)
+    return cache
+
+
+def _largest_weight(cache, q, e):
+    """[rows, Hq, 1]: each row's largest weight (of every key the last row sees)."""
+    G = q.shape[1] // cache.Hkv
+    sc, mn = ref.unpack(cache.k_codes, cache.k_params, "k")
+    x = torch.einsum("rhgd,hnd->rhgn", q.double().unflatten(1, (cache.Hkv, G)), sc + mn)
+    top = x.amax(-1).flatten(1) / math.sqrt(ref.D)
+    return torch.exp(top - e.lse).clamp(max=1.0)[..., None]
+
+
+def _check_attend(cache, q, dtype, sel=None, weights=False):
+    """Against the definition.  Weights enter the value product rounded to fp16 with
+    the row's largest at 2^12 or more: 2^-11 each, or half a step of 2^-24 below
+    2^-14, i.e. 2^-37 of the largest weight, times |min|.  Times the scale the same,
+    the scale of its group's largest being 1/2 or more and codes up to 15: 2^-36 of
+    the largest weight times 15 scales."""
+    s = cache.capacity
+    Hq, Hkv, rows = q.shape[1], cache.Hkv, q.shape[0]
+    so = ref.offsets([(rows, s)])
+    at = binding.Attention(dtype, Hq=Hq, Hkv=Hkv)
+    out, lse = at.attend(cache, q, so, sel_idx=sel, lse=True, weights=weights)
+    e, w, wt = ref.cache_expected(cache, q, [(rows, s)], so, sel)
+    n = s if sel is None else sel.shape[1]
+    part = cache.v_params.double().abs().amax(1)                       # [Hkv, 4, 2]
+    far = n * 2.0 ** -36 * (15 * part[..., 0] + part[..., 1])
+    far = far.repeat_interleave(32, 1).repeat_interleave(Hq // Hkv, 0) * _largest_weight(cache, q, e)
+    u = ref.half_step(ref.DTYPES[dtype])
+    tol = u * e.out.abs() + (2.0 ** -11 + 2 * e.dx[..., None] + 2.0 ** -18) * e.A + far
+    tol = tol + torch.finfo(ref.DTYPES[dtype]).smallest_normal * 2 * u
+    err = (out.double() - e.out).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert ((lse.double() - e.lse).abs() <= e.dx + 2.0 ** -20 * (1 + e.lse.abs())).all()
+    if weights:
+        assert ((cache.weight.double() - w).abs() <= wt + 2.0 ** -23 * w * (Hq + 8)).all()
+    return out, e
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,rows,selected", [(8, 1, False), (8, 1, True), (16, 1, False), (16, 1, True),
+                                              (32, 1, False), (8, 4, False), (32, 1, True)])
+@pytest.mark.parametrize("gap", [20.5, 24.5, 25.9, 30.6])
+def test_attend_many_keys_far_below_the_maximum_add_up(dtype, Hq, rows, selected, gap):
+    """One key in 16 at the maximum with values of zero, so that every warp has some;
+    the others 2^-gap below carry the values."""
+    t, n = ref.DTYPES[dtype], 4096
+    q = torch.zeros((rows, Hq, ref.D), dtype=t, device="cuda")
+    q[..., 0] = 8.0
+    k = torch.zeros((n, 1, ref.D), device="cuda")
+    k[::16, :, 0] = gap * math.log(2) * math.sqrt(ref.D) / 8
+    v = ref.vectors(n, 1, 3, torch.float32).abs() * 4 + 1
+    v[::16] = 0
+    cache = _cache_of(k, v)
+    sel = torch.arange(n, dtype=torch.int32, device="cuda").expand(rows, n).contiguous() if selected else None
+    out, e = _check_attend(cache, q, dtype, sel, weights=True)
+    if gap < 26 and dtype == "bf16":       # (fp16's own steps are 2^-24)
+        u = ref.half_step(t)
+        assert ((out.double() - e.out).abs() <= (u + 2.0 ** -9) * e.out.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,rows", [(8, 1), (16, 1), (8, 4)])
+@pytest.mark.parametrize("spread", [10, 22, 28])
+def test_attend_value_groups_of_very_different_sizes(dtype, Hq, rows, spread):
+    """Each group of a token's dimensions 2^spread / 3 times smaller than the last."""
+    t, n = ref.DTYPES[dtype], 900
+    q, k = ref.vectors(rows, Hq, 1, t), ref.vectors(n, 1, 2, t)
+    v = ref.vectors(n, 1, 3, torch.float32) * 500
+    v = v * torch.exp2(-spread / 3 * torch.arange(4, device="cuda").repeat_interleave(32))
+    for x in (v, v.flip(-1), v[:1].expand(n, 1, ref.D)):   # (equal scales round alike)
+        _check_attend(_cache_of(k, x), q, dtype)
+
+
+@pytest.mark.parametrize("G", [8, 16])
+def test_attend_an_infinite_scale_does_not_hide_the_finite_ones(G):
+    """A token that only the last row sees has an infinite value scale; the scales
+    beside it, 2^16 times the first ones, must reach the other rows whole.  So many
+    heads that the keys are not split: token 256 is the first warp's again."""
+    t, n, rows, Hkv = torch.bfloat16, 272, 2, 256
+    q, k = ref.vectors(rows, G * Hkv, 1, t), ref.vectors(n, Hkv, 2, t)
+    v = ref.vectors(n, Hkv, 3, torch.float32) * 0.01
+    v[256:] *= 2.0 ** 16
+    cache = _cache_of(k, v)
+    at, so = binding.Attention("bf16", Hq=G * Hkv, Hkv=Hkv), ref.offsets([(rows, n)])
+    want = at.attend(cache, q, so)
+    cache.v_params[:, n - 1, :, 0] = math.inf
+    out = at.attend(cache, q, so)
+    assert torch.isfinite(want).all() and torch.equal(out[0], want[0])
+    assert not torch.isfinite(out[1]).any()

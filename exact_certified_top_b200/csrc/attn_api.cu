@@ -531,8 +531,8 @@ dosa_status dosa_attn_prompt(dosa_attn_t hh, const dosa_rows* q, const dosa_rows
     if (launch_prompt(*h, rows16(q), rows16(k), rows16(v), Tq, S, t, rows16(out), lse, part_o,
                       part_lse, static_cast<int*>(workspace), stream) != cudaSuccess)
       return DOSA_ERR_CUDA;
-    if (launch_join(*h, join_table(t, h->cfg.Hq), rows16(out), lse, nullptr, part_o, part_lse,
-                    stream) != cudaSuccess)
+    if (launch_join(*h, DOSA_KERNEL_PROMPT, join_table(t, h->cfg.Hq), rows16(out), lse, nullptr,
+                    part_o, part_lse, stream) != cudaSuccess)
       return DOSA_ERR_CUDA;
   }
   return DOSA_OK;
@@ -657,7 +657,8 @@ dosa_status dosa_cache4_attend(dosa_attn_t hh, const dosa_cache4* cache, const d
                         scores, stream) != cudaSuccess)
         return DOSA_ERR_CUDA;
       const AttnTable j = join_table(t, h->cfg.Hq);
-      if (launch_join(*h, j, rows16(out), lse, lse2, part_o, part_lse, stream) != cudaSuccess)
+      if (launch_join(*h, DOSA_KERNEL_ATTEND, j, rows16(out), lse, lse2, part_o, part_lse, stream) !=
+          cudaSuccess)
         return DOSA_ERR_CUDA;
       const cudaError_t we =
           !add_weights ? cudaSuccess

@@ -120,9 +120,10 @@ cudaError_t launch_prompt(const AttnHandle& h, const Rows16& q, const Rows16& k,
                           int64_t q_rows, int64_t k_rows, const AttnTable& t, const Rows16& out,
                           float* lse, float* part_o, float* part_lse, int* err,
                           cudaStream_t stream);
-// Join split sequences: `rows` of the table's split sequences x Hq vectors.
-cudaError_t launch_join(const AttnHandle& h, const AttnTable& t, const Rows16& out, float* lse,
-                        float* lse2, const float* part_o, const float* part_lse,
+// Join split sequences: `rows` of the table's split sequences x Hq vectors.  kind:
+// the dosa_kernel its time counts for.
+cudaError_t launch_join(const AttnHandle& h, int kind, const AttnTable& t, const Rows16& out,
+                        float* lse, float* lse2, const float* part_o, const float* part_lse,
                         cudaStream_t stream);
 cudaError_t launch_cache_append(const AttnHandle& h, const Cache4View& c, const Rows16& k,
                                 const Rows16& v, const AttnTable& t, cudaStream_t stream);

@@ -1174,8 +1174,8 @@ cudaError_t launch_attend(const AttnHandle& h, const Cache4View& c, const Rows16
   return e;
 }
 
-cudaError_t launch_join(const AttnHandle& h, const AttnTable& t, const Rows16& out, float* lse,
-                        float* lse2, const float* part_o, const float* part_lse,
+cudaError_t launch_join(const AttnHandle& h, int kind, const AttnTable& t, const Rows16& out,
+                        float* lse, float* lse2, const float* part_o, const float* part_lse,
                         cudaStream_t stream) {
   if (t.units <= 0) return cudaSuccess;
   JoinParams p;
@@ -1186,8 +1186,11 @@ cudaError_t launch_join(const AttnHandle& h, const AttnTable& t, const Rows16& o
   p.part_lse = part_lse;
   p.Hq = h.cfg.Hq;
   const unsigned grid = (unsigned)((t.units + 7) / 8);
-  return h.fp16 ? launch_after(join_kernel<true>, dim3(grid), 256, 0, stream, t, p)
-                : launch_after(join_kernel<false>, dim3(grid), 256, 0, stream, t, p);
+  profile_before(kind, stream);
+  const cudaError_t e = launch_after(h.fp16 ? join_kernel<true> : join_kernel<false>, dim3(grid), 256,
+                                     0, stream, t, p);
+  profile_after(kind, stream);
+  return e;
 }
 
 cudaError_t launch_attend_weights(const AttnHandle& h, const Cache4View& c, const Rows16& q,
@@ -1266,9 +1269,11 @@ cudaError_t launch_list_weights(const AttnHandle& h, const AttnTable& t, const i
   profile_before(DOSA_KERNEL_ATTEND, stream);
   cudaError_t e = launch_after(weights_list_kernel, dim3(units), kListThreads, 0, stream, b, scores,
                                lse2, sel, K, h.cfg.Hq, row_weight, weight);
-  if (e == cudaSuccess && several)
-    e = launch_after(weights_scatter_kernel, dim3(b.n), kScatterThreads, 0, stream, b, sel, K,
-                     (const float*)row_weight, weight);
+  profile_after(DOSA_KERNEL_ATTEND, stream);
+  if (e != cudaSuccess || !several) return e;
+  profile_before(DOSA_KERNEL_ATTEND, stream);
+  e = launch_after(weights_scatter_kernel, dim3(b.n), kScatterThreads, 0, stream, b, sel, K,
+                   (const float*)row_weight, weight);
   profile_after(DOSA_KERNEL_ATTEND, stream);
   return e;
 }

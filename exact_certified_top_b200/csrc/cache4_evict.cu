@@ -264,12 +264,13 @@ cudaError_t launch_evict(const AttnHandle& h, const Cache4View& src, const Cache
   profile_before(DOSA_KERNEL_EVICT, stream);
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, t, (const float*)src.weight, first, last, kept,
                          kept_ld);
-  if (e == cudaSuccess && t.total > 0) {
-    const dim3 grid((unsigned)(((int64_t)t.total * 4 + kMoveThreads - 1) / kMoveThreads),
-                    (unsigned)h.cfg.Hkv);
-    e = launch_after(evict_move_kernel, grid, kMoveThreads, 0, stream, t, src, dst,
-                     (const int32_t*)kept, kept_ld);
-  }
+  profile_after(DOSA_KERNEL_EVICT, stream);
+  if (e != cudaSuccess || t.total == 0) return e;
+  const dim3 grid((unsigned)(((int64_t)t.total * 4 + kMoveThreads - 1) / kMoveThreads),
+                  (unsigned)h.cfg.Hkv);
+  profile_before(DOSA_KERNEL_EVICT, stream);
+  e = launch_after(evict_move_kernel, grid, kMoveThreads, 0, stream, t, src, dst,
+                   (const int32_t*)kept, kept_ld);
   profile_after(DOSA_KERNEL_EVICT, stream);
   return e;
 }

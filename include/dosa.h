@@ -496,7 +496,8 @@ typedef enum {
   DOSA_KERNEL_RANK = 12,       /* ranked screening: estimates and bound passes  */
   DOSA_KERNEL_PROMPT = 13,     /* prompt attention: scorer and joining          */
   DOSA_KERNEL_CACHE = 14,      /* 4-bit cache: append and read                  */
-  DOSA_KERNEL_ATTEND = 15,     /* attention over the 4-bit cache                */
+  DOSA_KERNEL_ATTEND = 15,     /* attention over the 4-bit cache: scorer,       */
+                               /* joining, recorded weights                     */
   DOSA_KERNEL_EVICT = 16,      /* eviction: selection and move                  */
   DOSA_KERNEL_KINDS = 17
 } dosa_kernel;

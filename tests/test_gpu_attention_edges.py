@@ -192,3 +192,37 @@ def test_attend_an_infinite_scale_does_not_hide_the_finite_ones(G):
     out = at.attend(cache, q, so)
     assert torch.isfinite(want).all() and torch.equal(out[0], want[0])
     assert not torch.isfinite(out[1]).any()
+
+
+def test_profile_counts_every_kernel_of_the_attention_calls():
+    """Split calls record their joining kernel; a selection with weights of one and
+    of several rows, and an eviction, each of theirs."""
+    t, Hq, Hkv, n = torch.bfloat16, 8, 1, 9000
+    at = binding.Attention("bf16", Hq=Hq, Hkv=Hkv)
+    q, k, v = ref.vectors(2, Hq, 1, t), ref.vectors(n, Hkv, 2, t), ref.vectors(n, Hkv, 3, t)
+    cache = binding.Cache4.empty(Hkv, n)
+    dst = binding.Cache4.empty(Hkv, 64)
+    whole, short = ref.offsets([(n, n)]), ref.offsets([(1, 5)])
+    one, two = ref.offsets([(1, n)]), ref.offsets([(2, n)])
+    sel = torch.arange(2048, dtype=torch.int32, device="cuda").expand(2, 2048).contiguous()
+    calls = [
+        (lambda: at.prompt(q, k, v, short), "prompt", 1),
+        (lambda: at.prompt(q, k, v, one), "prompt", 2),
+        (lambda: at.append(cache, k, v, whole), "cache", 1),
+        (lambda: at.attend(cache, q, short), "attend", 1),
+        (lambda: at.attend(cache, q, one), "attend", 2),
+        (lambda: at.attend(cache, q, two, weights=True), "attend", 3),
+        (lambda: at.attend(cache, q, one, sel_idx=sel[:1], weights=True), "attend", 3),
+        (lambda: at.attend(cache, q, two, sel_idx=sel, weights=True), "attend", 4),
+        (lambda: at.evict(cache, dst, [[0, n, 0, 64]]), "evict", 2),
+    ]
+    try:
+        binding.profile_enable(True)
+        for i, (call, kind, kernels) in enumerate(calls):
+            binding.profile_reset()
+            call()
+            torch.cuda.synchronize()
+            got = {name: c for name, (c, _) in binding.profile_read().items() if c}
+            assert got == {kind: kernels}, (i, got)
+    finally:
+        binding.profile_enable(False)

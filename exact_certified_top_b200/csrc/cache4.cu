@@ -124,18 +124,34 @@ __global__ void __launch_bounds__(kMaxThreads, 4) append_kernel(const __grid_con
   const float s = __half2float(hs), m = __half2float(hm);
   uint32_t w[4] = {0, 0, 0, 0};                    // dimensions 32 g + 8 i .. + 7
   if (!nan && s > 0.f) {
-    // The quotient (x - min) / scale rounded to fp32: a product with the rounded
-    // reciprocal and one correction by the exact remainder (P. Markstein,
-    // "Computation of elementary functions on the IBM RISC System/6000
-    // processor", 1990: correctly rounded from a correctly rounded reciprocal).
-    // Adding 1.5 2^23 rounds it to an integer (ties to even) in the sum's low bits.
+    // The quotient (x - min) / scale, rounded to fp32 on its way to the integer: a
+    // product with the rounded reciprocal and one correction by the exact remainder
+    // (P. Markstein, "Computation of elementary functions on the IBM RISC
+    // System/6000 processor", 1990: correctly rounded from a correctly rounded
+    // reciprocal).  Adding 1.5 2^23 rounds it to an integer (ties to even) in the sum's low bits.
     constexpr float kMagic = 12582912.f;
     const float r = __frcp_rn(s);
     // codes leave 0..15 only where the rounding of min or scale is not small
     // against the scale: then every quotient is clamped first
     const bool clamp = __fsub_rn(lo, m) * r < -0.49f || __fsub_rn(hi, m) * r > 15.49f;
+    // x - min is not exact in fp32 where one of them is below 2^-13 of the other, and
+    // its rounding may meet a half-integer multiple of the scale that x - min itself
+    // misses.  Rounded to odd it never does (such a multiple has fewer bits), and the
+    // quotient of a difference that misses misses the half by more than its own
+    // rounding.  Only two kinds of group can need it: minima next to a half-integer
+    // multiple of the scale (x is then the small one: below 2^-16 of the minimum in
+    // bf16, where only the multiple itself is near enough, 2^-13 in fp16), and minima
+    // that are small against the maximum.
+    constexpr float kNear = kFp16 ? 0x1p-11f : 0x1p-15f;
+    const float near = fmaf(-2.f * m, r, kMagic) - kMagic;   // halves of a scale in -min
+    const bool odd = fabsf(fmaf(near, s, 2.f * m)) <= kNear * fabsf(m) ? m != 0.f
+                                                                      : fabsf(m) * 4096.f < hi;
     auto code = [&](float x, bool hold) {
-      const float d = __fsub_rn(x, m);
+      float d = __fsub_rn(x, m);
+      if (hold) {
+        const float lower = __fsub_rd(x, m), upper = __fsub_ru(x, m);
+        if (lower != upper) d = __float_as_uint(lower) & 1u ? lower : upper;
+      }
       float q = d * r;
       q = fmaf(fmaf(-q, s, d), r, q);
       if (hold) q = fminf(fmaxf(q, 0.f), 15.f);
@@ -154,7 +170,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) append_kernel(const __grid_con
         w[i] = sum - 0x4B400000u * 0x11111111u;
       }
     };
-    if (clamp) encode(true);
+    if (clamp || odd) encode(true);
     else encode(false);
   }
   // transpose: lane c gets word c of every group

@@ -404,8 +404,9 @@ dosa_status dosa_attn_prompt_workspace_size(dosa_attn_t h, const int64_t* seq_of
  * Keys and values of `capacity` token slots, 80 bytes per vector instead of
  * 256.  Each group of 32 dimensions (dimension / 32) has scale = (max - min) /
  * 15 and min, both rounded to fp16 (the quotient to fp32 first), and as 4-bit
- * codes the integers nearest to the fp32 quotients (x - min) / scale (ties to
- * even, clamped to 0..15; 0 where scale is 0): a value is scale * code + min.  A group that
+ * codes the integers nearest to the exact quotients (x - min) / scale of the
+ * rounded min and scale (ties to even, clamped to 0..15; 0 where scale is 0): a
+ * value is scale * code + min.  A group that
  * holds a value that is not finite, or whose min or scale is beyond fp16's
  * range, reads back as NaN.
  *   codes  [Hkv][capacity][64] bytes, low nibble first.  Nibble n of a key holds

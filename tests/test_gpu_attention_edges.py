@@ -2,6 +2,7 @@
 another, infinite scores, weights far below a row's largest, value groups of very
 different sizes, quotients next to a half.  Bounds: attn_ref."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -226,3 +227,74 @@ def test_profile_counts_every_kernel_of_the_attention_calls():
             assert got == {kind: kernels}, (i, got)
     finally:
         binding.profile_enable(False)
+
+
+def _near_halves(dtype, n, seed):
+    """[n, 32] groups whose elements lie next to, or on, the half-integer multiples
+    of their scale: lo and hi random, the others the 16-bit numbers around
+    min + (i + 1/2) scale."""
+    t = ref.DTYPES[dtype]
+    g = torch.Generator().manual_seed(seed)
+    lo = -(torch.rand(n, generator=g) * 8 + 0.1)
+    hi = torch.rand(n, generator=g) * 8 + 0.1
+    few = torch.arange(n) % 3 == 0                    # few bits: many exact multiples
+    unit = torch.exp2(torch.randint(-3, 3, (n,), generator=g).float())
+    odd = 2 * torch.randint(0, 15, (n,), generator=g) + 1
+    k = torch.tensor([1.0, 3.0, 5.0, 7.0])[torch.randint(0, 4, (n,), generator=g)] * unit
+    lo, hi = torch.where(few, -odd / 2 * k, lo), torch.where(few, (15 - odd / 2) * k, hi)
+    lo, hi = lo.to(t), hi.to(t)
+    scale = ((hi.float() - lo.float()) / torch.full((n,), 15.0)).half().double()
+    mn = lo.half().double()
+    x = torch.empty((n, 32), dtype=t)
+    x[:, 0], x[:, 1] = lo, hi
+    for i in range(15):
+        at = mn + (i + 0.5) * scale
+        x[:, 2 + 2 * i] = at.to(t)
+        x[:, 3 + 2 * i] = (at + torch.where(torch.rand(n, generator=g) < 0.5, 1.0, -1.0) *
+                           torch.exp2(-torch.randint(8, 100, (n,), generator=g).double())).to(t)
+    tiny = torch.exp2(-torch.randint(9, 100 if dtype == "bf16" else 24, (n, 32), generator=g).double())
+    tiny = tiny * (1 + torch.rand((n, 32), generator=g).double()) * torch.where(
+        torch.rand((n, 32), generator=g) < 0.5, 1.0, -1.0)
+    swap = (torch.rand((n, 32), generator=g) < 0.3) & (torch.arange(32) >= 2)
+    x = torch.where(swap, tiny.to(t), x)
+    small = torch.arange(n) % 5 == 4                  # minima small against the maximum
+    x[small, 0] = -tiny[small, 0].abs().to(t)
+    x[small, 1:] = x[small, 1:].abs()
+    return torch.minimum(torch.maximum(x, x[:, :1]), x[:, 1:2].abs())
+
+
+def _codes(x):
+    """The definition in exact arithmetic: (codes, scale, min) of one group."""
+    lo, hi = min(x), max(x)
+    f32 = torch.tensor([hi, lo], dtype=torch.float32)
+    scale = ((f32[0] - f32[1]) / torch.tensor(15.0)).half().item()
+    mn = torch.tensor(lo).half().item()
+    if scale == 0:
+        return [0] * len(x), scale, mn
+    q = [round((Fraction(v) - Fraction(mn)) / Fraction(scale)) for v in x]   # (ties to even)
+    return [min(15, max(0, c)) for c in q], scale, mn
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_rounds_the_exact_quotient(dtype):
+    t, n = ref.DTYPES[dtype], 2048
+    x = _near_halves(dtype, n, 3)
+    # a quotient of 3.4999999995 that is 3.5 in fp32, and one on either side of 14.5
+    x[0] = torch.tensor([-3.5, 11.5] + [-1e-9, 1e-9, 0.0] * 10, dtype=t)
+    x[1] = torch.tensor([-14.5, 0.5] + [-2.0 ** -23, 2.0 ** -23, 0.0] * 10, dtype=t)
+    rows = x.view(n // 4, 1, ref.D).cuda()
+    cache = binding.Cache4.empty(1, n // 4)
+    at = binding.Attention(dtype, Hq=1, Hkv=1)
+    at.append(cache, rows, rows.clone(), ref.offsets([(n // 4, n // 4)]))
+    want = [_codes(r) for r in x.double().tolist()]
+    codes = torch.tensor([w[0] for w in want])
+    params = torch.tensor([w[1:] for w in want], dtype=torch.float16)
+    plain = ref.quantise(rows, "k")[0]
+    for kind in "kv":
+        got = getattr(cache, kind + "_codes")[0].cpu()
+        nib = torch.stack((got & 15, got >> 4), -1).flatten(-2).long()
+        nib = nib[:, torch.argsort(ref.order(kind))].reshape(n, 32)
+        assert torch.equal(getattr(cache, kind + "_params")[0].cpu().view(n, 2), params)
+        assert torch.equal(nib, codes), int((nib != codes).sum())
+    # the fp32 quotient's rounding would differ in some of these groups
+    assert not torch.equal(plain, cache.k_codes)

@@ -569,7 +569,7 @@ dosa_status dosa_cache4_read(dosa_attn_t hh, const dosa_cache4* cache, const int
 dosa_status dosa_cache4_attend_workspace_size(dosa_attn_t hh, const int64_t* seq_offsets, int B,
                                               int K, int add_weights, size_t* bytes) {
   const AttnHandle* h = handle(hh);
-  if (!h || !bytes || K < 0) return DOSA_ERR_INVALID_ARG;
+  if (!h || !bytes || K < 0 || K > kMaxRows) return DOSA_ERR_INVALID_ARG;
   const dosa_status st = check_batch(seq_offsets, B);
   if (st != DOSA_OK) return st;
   Plan plans[kWidths];

@@ -561,11 +561,8 @@ class Attention:
             raise ValueError(f"kept must be a contiguous int32 [{B}, keep] tensor")
         if kept.get_device() != dev:
             _on_current_device(kept=kept)
-        ld = kept.shape[1]
-        if ld == 0:
-            return kept
         _check("dosa_cache4_evict", self._lib.dosa_cache4_evict(
-            self._h, sa, da, at, B, first, last, kept.data_ptr(), ld, _stream(dev)))
+            self._h, sa, da, at, B, first, last, kept.data_ptr(), kept.shape[1], _stream(dev)))
         return kept
 
 

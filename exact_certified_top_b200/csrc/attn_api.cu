@@ -676,8 +676,8 @@ dosa_status dosa_cache4_evict(dosa_attn_t hh, const dosa_cache4* src, const dosa
                               const int64_t* spans, int B, int64_t first, int64_t last,
                               int32_t* kept_idx, int64_t kept_ld, void* stream) {
   const AttnHandle* h = handle(hh);
-  if (!h || !cache_ok(src) || !cache_ok(dst) || !src->weight || !spans || B < 1 || !kept_idx ||
-      !aligned(kept_idx, 4) || first < 0 || last < 0 || first > kMaxRows || last > kMaxRows ||
+  if (!h || !cache_ok(src) || !cache_ok(dst) || !src->weight || !spans || B < 1 ||
+      (!kept_idx && kept_ld != 0) || !aligned(kept_idx, 4) || first < 0 || last < 0 || first > kMaxRows || last > kMaxRows ||
       kept_ld < 0)
     return DOSA_ERR_INVALID_ARG;
   const size_t Hkv = (size_t)h->cfg.Hkv;
@@ -714,6 +714,7 @@ dosa_status dosa_cache4_evict(dosa_attn_t hh, const dosa_cache4* src, const dosa
       if (s[2] < o[2] + ok && o[2] < s[2] + kept) return DOSA_ERR_INVALID_ARG;
     }
   }
+  if (kept_ld == 0) return DOSA_OK;                // nothing is kept or listed
   EvictTable t;
   for (int b = 0; b < B;) {
     t.n = 0;

@@ -464,7 +464,7 @@ dosa_status dosa_cache4_attend_workspace_size(dosa_attn_t h, const int64_t* seq_
  * everything when its sign bit is clear and below when it is set) fill up to
  * keep.  The kept tokens move in order, with their weights, to dst slots
  * dst_start..; kept_idx [B, kept_ld] int32 lists them ascending (relative to
- * src_start), padded with -1.  The arrays of dst must not overlap those of src,
+ * src_start), padded with -1 (NULL where kept_ld is 0).  The arrays of dst must not overlap those of src,
  * nor the spans' dst slots one another; more than 4,096 spans have to ascend in
  * dst_start (UNSUPPORTED). */
 dosa_status dosa_cache4_evict(dosa_attn_t h, const dosa_cache4* src, const dosa_cache4* dst,

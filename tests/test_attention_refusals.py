@@ -22,3 +22,35 @@ def test_lists_longer_than_a_call_takes_have_no_workspace_size(lib, K):
     assert e.value.code == 1
     assert _call(lib, "attend", at, sel=FAKE, K=K) == 1
     assert at.attend_workspace_size([[0, 0, 30], [2, 40, 0]], K=1 << 30) > 0
+
+
+def test_evictions_that_keep_nothing_are_checked_like_others(lib):
+    """A result of no columns needs no address, and wrong spans stay wrong."""
+    at = binding.Attention(**SMALL)
+    nothing = [[0, 40, 0, 0], [40, 0, 3, 0]]
+    assert _evict(lib, at, nothing, kept=None, ld=0) == 0
+    assert _evict(lib, at, nothing, kept=FAKE, ld=0) == 0
+    assert _evict(lib, at, [[0, 40, 0, 20]], kept=None, ld=0) == 1
+    assert _evict(lib, at, nothing, kept=None, ld=0, first=1) == 1     # more than keep
+    for spans in ([[0, 65, 0, 0]], [[-1, 4, 0, 0]], [[0, -4, 0, 0]], [[0, 4, 0, -2]], [[0, 4, 65, 0]]):
+        assert _evict(lib, at, spans, kept=None, ld=0) == 1, spans
+    assert _evict(lib, at, nothing, kept=None, ld=4) == 1
+    assert _evict(lib, at, nothing, kept=None, ld=-1) == 1
+
+
+@pytest.fixture
+def host_as_device(monkeypatch):
+    """Host tensors pass for the current device's: what is refused is refused
+    before anything would be launched."""
+    monkeypatch.setattr(binding.torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(binding, "_stream", lambda dev=None: None)
+
+
+def test_the_binding_checks_evictions_that_keep_nothing(host_as_device):
+    at = binding.Attention(Hq=8, Hkv=2)
+    src, dst = (binding.Cache4.empty(2, 64, device="cpu") for _ in range(2))
+    assert at.evict(src, dst, [[0, 40, 0, 0]]).shape == (1, 0)
+    for spans, first in (([[0, 65, 0, 0]], 0), ([[0, 40, 0, 0]], 1), ([[0, 4, 0, -2]], 0)):
+        with pytest.raises(binding.DosaError) as e:
+            at.evict(src, dst, spans, first=first)
+        assert e.value.code == 1

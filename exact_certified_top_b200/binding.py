@@ -329,6 +329,14 @@ def _on_current_device(**tensors):
     return dev
 
 
+def _own_bytes(workspace, dev):
+    """The kernels take a caller's workspace as one run of bytes on their device."""
+    if workspace.get_device() != dev:
+        _on_current_device(workspace=workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 _Pair = ctypes.c_int64 * 2
 
 
@@ -463,11 +471,11 @@ class Attention:
         ws = workspace
         if ws is None:
             ws = q.new_zeros(self._prompt_ws(so, at, B), dtype=torch.uint8)
-        elif ws.get_device() != dev:
-            _on_current_device(workspace=ws)
+        else:
+            _own_bytes(ws, dev)
         _check("dosa_attn_prompt", self._lib.dosa_attn_prompt(
             self._h, qr, kr, vr, at, B, self._rows("out", out, Hq, Tq, dev), lse_at,
-            ws.data_ptr(), ws.numel(), _stream(dev)))
+            ws.data_ptr(), ws.nbytes, _stream(dev)))
         return out if lse is None else (out, lse)
 
     def append(self, cache: Cache4, k, v, seq_offsets):
@@ -533,11 +541,11 @@ class Attention:
         ws = workspace
         if ws is None:
             ws = q.new_zeros(self._attend_ws(so, at, B, K, weights), dtype=torch.uint8)
-        elif ws.get_device() != dev:
-            _on_current_device(workspace=ws)
+        else:
+            _own_bytes(ws, dev)
         _check("dosa_cache4_attend", self._lib.dosa_cache4_attend(
             self._h, arrays, qr, at, B, sel_at, K, 1 if weights else 0,
-            self._rows("out", out, Hq, Tq, dev), lse_at, ws.data_ptr(), ws.numel(), _stream(dev)))
+            self._rows("out", out, Hq, Tq, dev), lse_at, ws.data_ptr(), ws.nbytes, _stream(dev)))
         return out if lse is None else (out, lse)
 
     def evict(self, src: Cache4, dst: Cache4, spans, first: int = 0, last: int = 0, kept=None):

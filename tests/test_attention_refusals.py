@@ -54,3 +54,23 @@ def test_the_binding_checks_evictions_that_keep_nothing(host_as_device):
         with pytest.raises(binding.DosaError) as e:
             at.evict(src, dst, spans, first=first)
         assert e.value.code == 1
+
+
+@pytest.mark.parametrize("op", ["prompt", "attend"])
+def test_workspaces_with_gaps_are_refused(host_as_device, op):
+    """The call takes a workspace as one run of bytes: those between a view's
+    elements, and behind the last, are someone else's."""
+    at = binding.Attention(Hq=8, Hkv=2)
+    so = [[0, 0, 29], [1, 30, 0]]
+    q, k = torch.zeros((1, 8, 128), dtype=torch.bfloat16), torch.zeros((30, 2, 128), dtype=torch.bfloat16)
+    cache = binding.Cache4.empty(2, 30, device="cpu")
+    call = (lambda ws: at.prompt(q, k, k, so, workspace=ws)) if op == "prompt" else \
+        (lambda ws: at.attend(cache, q, so, workspace=ws))
+    size = at.prompt_workspace_size(so) if op == "prompt" else at.attend_workspace_size(so)
+    room = torch.zeros(4 * size, dtype=torch.uint8)
+    for ws in (room[::2], room.view(4, size)[:, :size // 2], room.view(-1, 2)[:, 0]):
+        with pytest.raises(ValueError, match="contiguous"):
+            call(ws)
+    with pytest.raises(binding.DosaError) as e:            # bytes count, not elements
+        call(torch.zeros(size // 4 - 1, dtype=torch.float32))
+    assert e.value.code in (1, 3)

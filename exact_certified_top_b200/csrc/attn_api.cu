@@ -595,6 +595,8 @@ dosa_status dosa_cache4_attend(dosa_attn_t hh, const dosa_cache4* cache, const d
   Plan plans[kWidths];
   const Layout L = layout(h, attend_plans(h, seq_offsets, B, K, plans), Tq, K, add_weights != 0);
   if (ws_bytes < L.total) return DOSA_ERR_WORKSPACE;
+  // the weights over every key read q again when out has been written
+  if (add_weights && !sel_idx && Tq > 0 && out->ptr == q->ptr) return DOSA_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* part_o = reinterpret_cast<float*>(ws + L.part_o);
   float* part_lse = reinterpret_cast<float*>(ws + L.part_lse);

@@ -446,7 +446,9 @@ dosa_status dosa_cache4_read(dosa_attn_t h, const dosa_cache4* cache, const int6
  * add_weights: after the call weight[slot] has grown by the sum over the
  * batch's rows and heads of p (rows in order, so results do not depend on
  * timing); needs cache->weight.  A row and head whose lse is -infinity adds
- * nothing.  lse (nullable) as in dosa_attn_prompt.
+ * nothing.  lse (nullable) as in dosa_attn_prompt.  out must not overlap q (the
+ * weights over every key read q again after out is written: INVALID_ARG for
+ * the same address there).
  * Workspace: dosa_cache4_attend_workspace_size of the same batch, K (0 without
  * sel_idx) and add_weights. */
 dosa_status dosa_cache4_attend(dosa_attn_t h, const dosa_cache4* cache, const dosa_rows* q,

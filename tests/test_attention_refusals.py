@@ -74,3 +74,13 @@ def test_workspaces_with_gaps_are_refused(host_as_device, op):
     with pytest.raises(binding.DosaError) as e:            # bytes count, not elements
         call(torch.zeros(size // 4 - 1, dtype=torch.float32))
     assert e.value.code in (1, 3)
+
+
+def test_recorded_weights_of_rows_that_out_replaces_are_refused(lib):
+    """Over every key the weights read the query rows again behind the result."""
+    at = binding.Attention(**SMALL)
+    assert _call(lib, "attend", at, add=1) == 1                        # out is q
+    assert _call(lib, "attend", at, add=1, out=_rows(ptr=FAKE + (1 << 20)), ws=None) == 1
+    assert _call(lib, "attend", at, add=1, out=_rows(ptr=FAKE + (1 << 20)), n=100) == 3
+    none = [[0, 0, 0], [0, 40, 0]]
+    assert _call(lib, "attend", at, none, add=1) == 0                  # no rows to replace

@@ -85,6 +85,14 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+
+// The fp16 pair w of a and b, with fp16's largest number where a finite one became
+// infinite.
+__device__ __forceinline__ uint32_t hold_finite(uint32_t w, float a, float b) {
+  if ((w & 0x7FFFu) == 0x7C00u && fabsf(a) < INFINITY) w -= 1u;
+  if ((w & 0x7FFF0000u) == 0x7C000000u && fabsf(b) < INFINITY) w -= 0x10000u;
+  return w;
+}
 #endif
 
 struct Rows16 {

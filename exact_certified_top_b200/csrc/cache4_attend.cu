@@ -830,6 +830,7 @@ struct JoinParams {
   float *lse, *lse2;
   const float *part_o, *part_lse;
   int Hq;
+  bool hold;         // fp16: finite means stay finite (prompt: no value is beyond fp16's end)
 };
 
 // One warp per (row, head) vector of a split sequence, 4 dimensions per lane.
@@ -878,6 +879,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnT
   if constexpr (kFp16) {
     o.x = pack_half(acc[0] * inv, acc[1] * inv);
     o.y = pack_half(acc[2] * inv, acc[3] * inv);
+    if (p.hold) {
+      o.x = hold_finite(o.x, acc[0] * inv, acc[1] * inv);
+      o.y = hold_finite(o.y, acc[2] * inv, acc[3] * inv);
+    }
   } else {
     const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
     const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
@@ -1185,6 +1190,7 @@ cudaError_t launch_join(const AttnHandle& h, int kind, const AttnTable& t, const
   p.part_o = part_o;
   p.part_lse = part_lse;
   p.Hq = h.cfg.Hq;
+  p.hold = kind == DOSA_KERNEL_PROMPT;
   const unsigned grid = (unsigned)((t.units + 7) / 8);
   profile_before(kind, stream);
   const cudaError_t e = launch_after(h.fp16 ? join_kernel<true> : join_kernel<false>, dim3(grid), 256,

@@ -897,11 +897,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32_async(to + b * 64 + 32, o[1]);
               tmem_wait_ld(o[0]);
               tmem_wait_ld(o[1]);
+              __half2 most = __float2half2_rn(0.f);
 #pragma unroll
               for (int f = 0; f < 8; ++f) {
                 const float* e = o[f >> 2] + (f & 3) * 8;
-                put(f, pack2<kFp16>(e[0] * mul, e[1] * mul), pack2<kFp16>(e[2] * mul, e[3] * mul),
-                    pack2<kFp16>(e[4] * mul, e[5] * mul), pack2<kFp16>(e[6] * mul, e[7] * mul));
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  w[i] = pack2<kFp16>(e[2 * i] * mul, e[2 * i + 1] * mul);
+                  if constexpr (kFp16)
+                    most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+                }
+                put(f, w[0], w[1], w[2], w[3]);
+              }
+              // A mean is no larger than its largest value, but weights that round up
+              // can carry one near fp16's end past it: what is finite stays so.  (In
+              // bf16 the last step before infinity is wider than that.)
+              if (kFp16 && __hgt2_mask(most, __float2half2_rn(65504.f))) {
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                  const float* e = o[f >> 2] + (f & 3) * 8;
+                  uint32_t w[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float x = e[2 * i] * mul, y = e[2 * i + 1] * mul;
+                    w[i] = hold_finite(pack2<kFp16>(x, y), x, y);
+                  }
+                  put(f, w[0], w[1], w[2], w[3]);
+                }
               }
               flush(b);
             }

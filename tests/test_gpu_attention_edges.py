@@ -298,3 +298,33 @@ def test_append_rounds_the_exact_quotient(dtype):
         assert torch.equal(nib, codes), int((nib != codes).sum())
     # the fp32 quotient's rounding would differ in some of these groups
     assert not torch.equal(plain, cache.k_codes)
+
+
+@pytest.mark.parametrize("rows,n", [(300, 300), (4, 9000), (1, 5)], ids=["whole", "split", "short"])
+def test_prompt_means_of_the_largest_values_stay_finite(rows, n):
+    """A mean is no larger than its largest value: rounding the weights up must not
+    push it over fp16's end; a visible infinity still does.  (Weights and result
+    round by 2^-11 each, so the mean may be that much smaller.)"""
+    t, Hq = torch.float16, 8
+    so = ref.offsets([(rows, n)])
+    far = torch.finfo(t).max
+    sign = torch.where(torch.arange(ref.D, device="cuda") % 3 == 0, -far, far).to(t)
+    k, v = ref.vectors(n, 1, 2, t), sign.expand(n, 1, ref.D).contiguous()
+    at = binding.Attention("fp16", Hq=Hq, Hkv=1)
+    near = lambda x: (x.double() / sign[:x.shape[-1]].double() - 1).abs() <= 2.0 ** -10 + 2.0 ** -17
+    for seed in range(8):
+        q = ref.vectors(rows, Hq, seed, t)
+        out = at.prompt(q, k, v, so)
+        assert near(out).all(), (seed, int(torch.isinf(out).sum()))
+    # from key 64 on weights of 1 + 2^-11 and a little of the maximum at hand: every one
+    # rounds up to 1 + 2^-10
+    q, k2 = torch.zeros_like(q), torch.zeros_like(k)
+    q[..., 0], k2[64:, 0, 0] = 1.0, math.log(1 + 1.02 * 2.0 ** -11) * math.sqrt(ref.D)
+    out = at.prompt(q, k2, v, so)
+    assert near(out).all(), int(torch.isinf(out).sum())
+    first = min(2, n - rows)
+    v[first, 0, 3], v[first, 0, 4] = math.inf, -math.inf
+    out = at.prompt(q, k, v, so)[max(0, first - (n - rows)):]
+    assert (out[..., 3] == math.inf).all()                 # (with -far beside it, in fp32)
+    assert (out[..., 4] == -math.inf).all()
+    assert near(out)[..., 5:].all()

@@ -3,7 +3,8 @@
 //
 // Both are memory work (256 bytes of rows and 80 of cache per vector) with
 // nearly as much to issue: 8,289 tokens of 8 heads are appended and read back in
-// 20 us, 12 for the bytes, with 62 and 58 % of the issue slots used.  Four
+// 20 us, 12 for the bytes, with 64 and 58 % of the issue slots used and warps that
+// mostly wait for loads: neither is full.  Four
 // lanes take one head vector and a warp 8 consecutive tokens of one head, so
 // the head-major cache is accessed in 512-byte runs of codes and 128-byte runs
 // of parameters.  Append: a lane quantises one group of 32 dimensions alone (no

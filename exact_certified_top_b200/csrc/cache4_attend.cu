@@ -25,14 +25,16 @@
 // move only when a score exceeds them by 2^kSlack, so most slices need no
 // rescaling.
 //
-// Bound: issue and memory together up to 8 columns (360 warp instructions per
-// slice of 16 tokens; one row of 64 heads over 1M keys takes 270 us with 70 % of
+// Bound: issue and memory together up to 8 columns (390 warp instructions per
+// slice of 16 tokens; one row of 64 heads over 1M keys takes 284 us with 72 % of
 // the issue slots used, 207 for the bytes), the latency of dependent products
-// beyond (790 instructions per slice at 32 columns, where registers leave 2
-// warps per scheduler: 4 rows 757 us).  Columns per unit: 8 with two CTAs per
-// SM, else 16 or 32 with one.  For 2 rows over 1M keys 16 columns took 375 us
-// with 8 warps and 255 registers, 395 with 12 warps and 168, 530 with two CTAs
-// and 128; for 4 rows two units of 16 columns took 1,045 against 757.
+// beyond (850 instructions per slice at 32 columns, where registers leave 2
+// warps per scheduler: 4 rows 773 us).  Weight times scale in fp32 costs 32 of the
+// 390 instructions: a product in fp16 took 267 us, but lost the bits of groups
+// and keys beside larger ones.  Columns per unit: 8 with two CTAs per SM, else 16
+// or 32 with one.  With that product, for 2 rows over 1M keys 16 columns took 375
+// us with 8 warps and 255 registers (388 now), 395 with 12 warps and 168, 530 with
+// two CTAs and 128; for 4 rows two units of 16 columns took 1,045 against 757.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1081,9 +1083,10 @@ __global__ void __launch_bounds__(kListThreads)
 }
 
 // Selection, sequences of several rows: the rows' sums go to the tokens they
-// list, rows in order (a CTA barrier between them).  Within a row a token listed
-// twice gets two equal additions, so their order does not matter.  The next
-// row's entries are loaded before the barrier.
+// list, 4,096 entries of every list at a time and the rows in order within them (a
+// CTA barrier between two rows).  Within a row a token listed twice gets two equal
+// additions, so their order does not matter.  The next row's entries are loaded
+// before the barrier.
 constexpr int kScatterThreads = 1024, kScatterEach = 4;
 __global__ void __launch_bounds__(kScatterThreads)
     weights_scatter_kernel(const __grid_constant__ AttnTable t, const int32_t* sel, int K,

@@ -32,11 +32,16 @@
 // rarely rescaled: P stays below 2^kSlack (2^(kSlack + kLift) in fp16), and sums are
 // fp32.  A CTA's roles wait on mbarriers only; every wait is bounded.
 //
-// Measured: 16,384 tokens, 64 heads over 8: 3.7 ms, 1.19 PFLOP/s for the 4.4
-// TFLOP below the diagonal (4.15 ms when the power cap holds the clock).  Per 64 keys of both tiles the softmax takes 1,210
-// of about 1,690 cycles and waits for the rest, the tensor core works 1,256:
-// neither is full, and the exponentials (a third of them on the FMA pipe) bound
-// what a better overlap could reach.
+// The softmax with a running maximum and sum is the online one of M. Milakov and
+// N. Gimelshein (2018).  The arrangement is that of published attention for this
+// tensor core: two row tiles that take turns, P over S in TMEM, a maximum that
+// moves only by more than 2^8, a share of the exponentials as polynomials.
+//
+// Measured: 16,384 tokens, 64 heads over 8: 3.65 ms, 1.2 PFLOP/s for the 4.4
+// TFLOP below the diagonal (4.2 ms when the power cap holds the clock).  Per 64
+// keys of both tiles the softmax takes 1,210 of about 1,690 cycles and waits for
+// the rest, the tensor core works 1,256: neither is full, and the exponentials (a
+// third of them on the FMA pipe) bound what a better overlap could reach.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -234,7 +239,7 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 // 2^x on the FMA pipe, x <= kSlack: x = n + f with n the nearest integer (taken
 // out of the low bits of x + 1.5 2^23), 2^f on [-1/2, 1/2] by the degree-4
 // polynomial of least relative error (2.6e-6, fitted by Remez exchange; P itself
-// rounds to 2^-12 or 2^-9), times 2^n.  x is held at -127, whose factor is a zero
+// rounds to 2^-11 or 2^-8), times 2^n.  x is held at -127, whose factor is a zero
 // of the bits: masked scores (-infinity) and what is below 2^-126.5 weigh nothing,
 // however large the value.  NaN stays: a score of +infinity is one here (infinity
 // minus the maximum it has become), and a zero in its place would drop the key

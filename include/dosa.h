@@ -444,7 +444,7 @@ dosa_status dosa_cache4_read(dosa_attn_t h, const dosa_cache4* cache, const int6
  * counts twice.  A row with no key gives zeros and lse = -infinity, one that sees
  * a score of +infinity or NaN gives NaN.
  * add_weights: after the call weight[slot] has grown by the sum over the
- * batch's rows and heads of p (rows in order, so results do not depend on
+ * batch's rows and heads of p (in a fixed order, so results do not depend on
  * timing); needs cache->weight.  A row and head whose lse is -infinity adds
  * nothing.  lse (nullable) as in dosa_attn_prompt.  out must not overlap q (the
  * weights over every key read q again after out is written: INVALID_ARG for
